@@ -11,12 +11,15 @@
 //                 (two k-steps per block and 8 tokens; the block's scale is a
 //                 factor of the whole dot product over the block, applied in
 //                 fp32 to the accumulators)
-//   O[16 x D] += P[16 x 16] . (vsc[t, b] Vcode), P as fp16 hi + lo (22 bits:
-//                 the fp32 outputs keep 1e-5)
+//   O[16 x D] += P[16 x 16] . (vsc[t, b] Vcode), P as fp16 hi + lo, 22
+//                 bits (one term would cost the fp32 outputs 2e-4)
 // The codes are the operands' own order in the tile (see the layout), so a
 // lane loads its share of 8 tokens with one 128-bit shared load and widens a
 // byte to an fp16 pair with one conversion; the 4-bit values are exact in
-// fp16. Queries are scaled per row by a power of two into fp16's range.
+// fp16. Queries are scaled per row by a power of two into fp16's range: their 8
+// bits stay exact down to 2^-17 of the row's largest value, and what is below is
+// off by 2^-25 of it, less than fp32's sum over the dims loses beside the
+// largest (a second term for it would double the score's MMAs).
 //
 // A CTA has two warps, each of which owns half the scale blocks, and takes its
 // run's tiles in rounds of two per warp. Warp w scores tiles 2 w and 2 w + 1 of
@@ -26,9 +29,11 @@
 // twice. On 32 sequences x 32K tokens x 64/4 heads of 128: 193 us with
 // the merge; one warp doing all of a tile by itself 253, a warp per block,
 // four in a CTA, 202 (each P and each line of value codes is read four times).
-// The rows' references (about their maxima) are common to the CTA: P may reach
-// 2^8, and only a score beyond that makes the warps exchange maxima and
-// rescale.
+// The warps exchange the rows' maxima over the round's 64 tokens, and P is held
+// relative to them, so that fp16's range serves the round and not the row: a
+// row's light tokens (behind a sink, say, 2^-25 of it each) keep their bits. The
+// round's P V enters O by one factor per row. O and the sums are in units of
+// 2^reference, which rises only with a score 2^40 above it.
 //
 // A value's scale belongs to one (token, 32 dims), so it can leave neither the
 // sum over tokens nor the sum over dims: it multiplies the fp16 codes. Scales
@@ -37,7 +42,8 @@
 // within 2^-14 .. 2^1 of the reference (checked four tokens at a time by one
 // subtraction) are normal fp16 powers of two, exactly. Any other tile (rare:
 // values of neighbouring tokens 2^14 apart) takes bf16 operands, whose range
-// holds every scale: codes as bf16 subnormals times 2^126, P as bf16 hi + lo.
+// holds every scale: codes as bf16 subnormals times 2^126, P as bf16 hi + lo
+// (16 bits; a third term for tiles this rare is not worth its registers).
 //
 // Bound: the tensor pipe and instruction issue together. Per SM quadrant an
 // m16n8k16 MMA takes 4.2 ns (8 cycles), and about half of it keeps other
@@ -48,9 +54,10 @@
 // are 97 ns of an SM that way, where its share of HBM delivers the 2,176 bytes
 // in 49 ns. Lanes of at most eight rows (HALF: one query token of up to eight
 // heads per KV head, say) put P's low terms into the MMA's upper rows, which are
-// empty, and leave the upper rows' scores alone: 32 MMAs, 173 us where 16 rows
-// take 193 (32 x 32K tokens, 4 KV heads). More warps change nothing: 193 us at 12 an SM (168 registers), 203
-// at 16 (128 registers, two stages).
+// empty, and leave the upper rows' scores alone: 32 MMAs, 177 us where 16 rows
+// take 193 (32 x 32K tokens, 4 KV heads; D = 128 spills 22 bytes a thread).
+// More warps change nothing: 193 us at 12 an SM (168 registers), 203 at 16 (128
+// registers, two stages).
 #include <cmath>
 #include <mutex>
 
@@ -62,6 +69,16 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// P at a round's maximum is 2^kHead: two fp16 terms, which end at 2^-24, then
+// hold 22 bits of a weight down to 2^-17 of that maximum, and are off by 2^-39
+// of it at most further below.
+constexpr float kHead = 14.f;
+// A row's reference, the unit of its O and sum, follows when a score is 2^kRise
+// above it. (fp32 has room for more; a rise costs a rescale of O.)
+constexpr float kRise = 40.f;
+// The reference of a row that has seen nothing: finite, so that differences of
+// two references are numbers or -inf, and 2^them 1 or 0.
+constexpr float kNone = -3e38f;
 
 template <int D>
 struct Mx4Cfg {
@@ -77,8 +94,8 @@ struct Mx4Cfg {
   static constexpr int kOffP = kStages * kStageBytes;   // the round's P: per tile hi and lo operands of 32 lanes
   static constexpr int kOffQ = kOffP + kTiles * 1024;   // the query rows as operands: 512 bytes a k-step
   static constexpr int kOffF = kOffQ + 16 * D * 2;      // the round's value factors: per tile, scale block and t4
-  static constexpr int kOffRed = kOffF + kTiles * kBlk * 32;  // per warp and row: a maximum or a sum
-  static constexpr int kOffTop = kOffRed + kWarps * 16 * 4;     // per warp and scale block: the largest scale code
+  static constexpr int kOffRed = kOffF + kTiles * kBlk * 32;  // per warp and row: four lanes' maxima, or a sum
+  static constexpr int kOffTop = kOffRed + kWarps * 16 * 16;    // per warp and scale block: the largest scale code
   static constexpr int kOffBar = kOffTop + kWarps * kBlk * 4;
   static constexpr int kOffTile = kOffBar + kStages * 8;        // per tile of the round, a byte: 0 none, else its tokens
   static constexpr int kOffAbort = kOffTile + 8;                // (+ 128: scales far apart)
@@ -419,11 +436,14 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
     }
     __syncthreads();
 
-    float o[4 * kOwn][4];  // rows gr, gr + 8 and dims 32 kOwn warp + 8 m + 2 t4, + 1
+    constexpr int kO = HALF ? 2 : 4;
+    float o[4 * kOwn][kO];  // rows gr, gr + 8 and dims 32 kOwn warp + 8 m + 2 t4, + 1
 #pragma unroll
-    for (int m = 0; m < 4 * kOwn; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-    // the rows' references in log2 units (-inf: nothing seen) and the sums of this lane's columns
-    float ref0 = -INFINITY, ref1 = -INFINITY, l[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    for (int m = 0; m < 4 * kOwn; ++m)
+#pragma unroll
+      for (int e = 0; e < kO; ++e) o[m][e] = 0.f;
+    // the rows' references in log2 units and the sums of this lane's columns
+    float ref0 = kNone, ref1 = kNone, l[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     // scale code of O's unit: of this warp's blocks, and of block gr % kBlk,
     // whose factors the lane makes; 15 or more, so that the codes within 14
     // below a unit are not negative
@@ -519,9 +539,12 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
                 else mx1 = fmaxf(mx1, s[j][h][e]);
               }
       }
-      // (a maximum of -inf is a row that sees none of the tokens)
-      mx0 = mx0 == -INFINITY ? mx0 : mx0 * rsl2[0];
-      mx1 = HALF ? mx0 : mx1 == -INFINITY ? mx1 : mx1 * rsl2[1];
+      // (a maximum of -inf is a row that sees none of the tokens; NaN, from a scale of 0, counts as that)
+      mx0 *= rsl2[0];
+      mx1 = HALF ? mx0 : mx1 * rsl2[1];
+      // (each lane's part of the maxima, for both warps: no shuffles before the barrier)
+      red[(warp * 16 + gr) * 4 + t4] = mx0;
+      if (!HALF) red[(warp * 16 + gr + 8) * 4 + t4] = mx1;
       // Value scales of block gr % kBlk, tokens 2 t4 and 2 t4 + 1 of either half:
       // bytes of z. Less (unit - 14) they are the factors' exponents, near if all
       // within 0 .. 15: 4 (x + 1) as a half's upper byte has the exponent field
@@ -548,17 +571,25 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
       }
       // every warp has left the round before (its P, factors and stage are free),
       // and knows whether a score is too high or a scale far from its unit
-      const bool high = __syncthreads_or(mx0 > ref0 + 8.f || mx1 > ref1 + 8.f || far != 0u);
+      const bool high = __syncthreads_or(mx0 > ref0 + kRise || mx1 > ref1 + kRise || far != 0u);
       if (*abort_flag) {  // (raised before the barrier: the same for all)
         stopped = i;
         break;
       }
       if (i > 0 && i + C::kStages - 1 < n_rounds) issue(i + C::kStages - 1);
+      // the rows' maxima in this round
+      float x0 = kNone, x1 = kNone;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) {
+        const float4 a = *reinterpret_cast<const float4*>(red + (w * 16 + gr) * 4);
+        x0 = max3f(max3f(x0, a.x, a.y), a.z, a.w);
+        if (!HALF) {
+          const float4 c = *reinterpret_cast<const float4*>(red + (w * 16 + gr + 8) * 4);
+          x1 = max3f(max3f(x1, c.x, c.y), c.z, c.w);
+        }
+      }
+      if (HALF) x1 = x0;
       if (high) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
         int top = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -566,11 +597,7 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
           for (int e = 0; e < 4; ++e) top = max(top, scale_of(z[j], e));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (t4 == 0) {
-          red[warp * 16 + gr] = mx0;
-          red[warp * 16 + gr + 8] = mx1;
-          if (gr < kBlk) tops[warp * kBlk + gr] = top;
-        }
+        if (t4 == 0 && gr < kBlk) tops[warp * kBlk + gr] = top;
         __syncthreads();
         // the units rise to the round's largest scales
         float down[kOwn];
@@ -584,15 +611,10 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
         }
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) unit_gr = max(unit_gr, tops[w * kBlk + blk]);
-        float x0 = ref0, x1 = ref1;
-#pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) {
-          x0 = fmaxf(x0, red[w * 16 + gr]);
-          x1 = fmaxf(x1, red[w * 16 + gr + 8]);
-        }
-        const float a0 = ref0 == -INFINITY ? 0.f : ex2_ftz(ref0 - x0), a1 = ref1 == -INFINITY ? 0.f : ex2_ftz(ref1 - x1);
-        ref0 = x0;
-        ref1 = x1;
+        const float top0 = fmaxf(ref0, x0), top1 = fmaxf(ref1, x1);
+        const float a0 = ex2_ftz(ref0 - top0), a1 = ex2_ftz(ref1 - top1);
+        ref0 = top0;
+        ref1 = top1;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           l[0][e] *= a0;
@@ -600,10 +622,8 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
         }
 #pragma unroll
         for (int m = 0; m < 4 * kOwn; ++m) {
-          o[m][0] *= a0 * down[m / 4];
-          o[m][1] *= a0 * down[m / 4];
-          o[m][2] *= a1 * down[m / 4];
-          o[m][3] *= a1 * down[m / 4];
+#pragma unroll
+          for (int e = 0; e < kO; ++e) o[m][e] *= (e < 2 ? a0 : a1) * down[m / 4];
         }
       }
       // the factors of this warp's tiles, all blocks
@@ -631,9 +651,12 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
         const int n = j ? n1 : n0;
         if (lane == 0) tile_info[2 * warp + j] = (unsigned char)(n <= 0 ? 0 : n | (apart ? 128 : 0));
       }
-      const float r0 = ref0 == -INFINITY ? 0.f : ref0, r1 = ref1 == -INFINITY ? 0.f : ref1;
-      // P of this warp's tiles
+      // P of this warp's tiles, 2^kHead at the round's maximum; in O's units that
+      // is size0, size1 times as much
+      const float r0 = x0 - kHead, r1 = x1 - kHead;
+      const float size0 = ex2_ftz(r0 - ref0), size1 = ex2_ftz(r1 - ref1);
       if (n0 + n1 > 0) {
+        float sum0[2] = {0.f, 0.f}, sum1[2] = {0.f, 0.f};
         const unsigned long long f0 = f2pack(rsl2[0], rsl2[0]), f1 = f2pack(rsl2[1], rsl2[1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -649,11 +672,11 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
 #pragma unroll
               for (int e = 0; e < (HALF ? 2 : 4); ++e) z[e] = sees(j, h, e) ? z[e] : 0.f;
             }
-            add2(l[0], z);
+            add2(sum0, z);
             if constexpr (HALF) {
               split_f16(z[0], z[1], pa[2 * h], pa[2 * h + 1]);
             } else {
-              add2(l[1], z + 2);
+              add2(sum1, z + 2);
               split_f16(z[0], z[1], pa[2 * h], pl[2 * h]);
               split_f16(z[2], z[3], pa[2 * h + 1], pl[2 * h + 1]);
             }
@@ -661,6 +684,8 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
           st_shared_v4(pbuf + (2 * warp + j) * 1024, pa[0], pa[1], pa[2], pa[3]);
           if (!HALF) st_shared_v4(pbuf + (2 * warp + j) * 1024 + 512, pl[0], pl[1], pl[2], pl[3]);
         }
+        fma2(l[0], sum0, f2pack(size0, size0));
+        if (!HALF) fma2(l[1], sum1, f2pack(size1, size1));
       }
       __syncthreads();  // the round's P and factors are there
       // the round's P V on accumulators of its own, added to O once: the MMA's
@@ -761,10 +786,12 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
           }
         }
       }
+      const unsigned long long by0 = f2pack(size0, size0), by1 = f2pack(size1, size1);
 #pragma unroll
       for (int m = 0; m < 4 * kOwn; ++m) {
-        add2(o[m], acc[m]);
-        add2(o[m] + 2, acc[m] + 2);
+        if constexpr (HALF) add2(acc[m], acc[m] + 2);  // P's low terms
+        fma2(o[m], acc[m], by0);
+        if constexpr (!HALF) fma2(o[m] + 2, acc[m] + 2, by1);
       }
     }
     if (stopped >= 0) {  // copies in flight must land before the CTA may leave
@@ -806,9 +833,7 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
 #pragma unroll
       for (int m = 0; m < 4 * kOwn; ++m) {
         const float size = __uint_as_float((uint32_t)unit[m / 4] << 23);
-        float x = o[m][2 * e], y = o[m][2 * e + 1];
-        if (HALF) x += o[m][2], y += o[m][3];  // (e = 0)
-        *reinterpret_cast<float2*>(out + 8 * m) = make_float2(x * inv * size, y * inv * size);
+        *reinterpret_cast<float2*>(out + 8 * m) = make_float2(o[m][2 * e] * inv * size, o[m][2 * e + 1] * inv * size);
       }
       if (t4 == 0 && warp == 0)
         (out_row >= 0 ? p.tmp_lse : p.lses)[row] = den == 0.f ? -INFINITY : ((e ? ref1 : ref0) + log2f(den)) * kLn2;
