@@ -29,6 +29,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// F8: P is 2^kF8Head at the row's maximum. It is fp16, whose range ends at 2^-24:
+// 11 bits down to 2^-29 of the maximum, 0 only below 2^-40 (with P at most 1,
+// tokens of 2^-25 of a heavy one counted as 0).
+constexpr float kF8Head = 15.f;
 constexpr float kLoFraction = 1.0f / 32.0f;  // F8: tile share of a row's weight above which P_lo . V is issued
 
 // F8: the cache holds FP8 E4M3 codes (1 byte per element) instead of bf16;
@@ -457,9 +461,10 @@ __global__ void __launch_bounds__(GqaCfg<D>::kThreads, (GqaCfg<D, F8, T>::kMinCt
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
       const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
       // reference maxima (a row with nothing seen yet keeps 0 to avoid inf - inf)
-      const float r0 = n0 == -INFINITY ? 0.f : n0;
-      const float r1 = n1 == -INFINITY ? 0.f : n1;
-      const float a0 = exp2_k<F8>(m0 - r0), a1 = exp2_k<F8>(m1 - r1);
+      const float c0 = n0 == -INFINITY ? 0.f : n0;
+      const float c1 = n1 == -INFINITY ? 0.f : n1;
+      const float a0 = exp2_k<F8>(m0 - c0), a1 = exp2_k<F8>(m1 - c1);
+      const float r0 = F8 ? c0 - kF8Head : c0, r1 = F8 ? c1 - kF8Head : c1;
       m0 = n0;
       m1 = n1;
       float p_[2][4];
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(GqaCfg<D>::kThreads, (GqaCfg<D, F8, T>::kMinCt
       }
       const size_t row = (size_t)js * js_rows + r;
       out_o[row * D + c] = den > 0.f ? (F8 ? num / den * p.v_scale : num / den) : 0.f;
-      if (c == 0) out_l[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+      if (c == 0) out_l[row] = den > 0.f ? ((F8 ? M - kF8Head : M) + log2f(den)) * kLn2 : -INFINITY;
     }
     __syncthreads();
   }

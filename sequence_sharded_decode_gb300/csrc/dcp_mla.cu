@@ -181,6 +181,11 @@ static_assert(kPrefetch >= 0 && kPrefetch <= 32, "prefetch distance within the t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
+// 8-bit cache: P is fp16, whose range ends at 2^-24. It is 2^kF8Head at the
+// row's reference and at most 2^(kF8Head + kF8Threshold): 11 bits down to 2^-25
+// of the reference, 0 only below 2^-36 (with P at most 2^8 and 1 at the
+// reference, tokens of 2^-25 of a heavy one counted as 0).
+constexpr float kF8Head = 11.0f, kF8Threshold = 4.0f;
 constexpr float kLoFraction = 1.0f / 32.0f;      // tile share of the row sum above which P_lo . V is issued
 
 struct MlaParams {
@@ -872,12 +877,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool rescale = false;
         if (m_run == -INFINITY) {
           m_new = mx;
-        } else if (mx > m_run + kRescaleThreshold) {
+        } else if (mx > m_run + (F8 ? kF8Threshold : kRescaleThreshold)) {
           m_new = mx;
           alpha = exp2f(m_run - m_new);
           rescale = true;
         }
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float ref = m_new == -INFINITY ? 0.f : F8 ? m_new - kF8Head : m_new;
         float sc[32];
         float lsum;
         {
@@ -1032,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // both computed the same scores and sums), so that each CTA's own count
       // below covers every LSE its merge reads.
       if (e == 0 && out_lse && (rank == 0 || piece))
-        *out_lse = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+        *out_lse = l_run > 0.f ? ((F8 ? m_run - kF8Head : m_run) + log2f(l_run)) * kLn2 : -INFINITY;
       tc_fence_before();
       gt += nt;
       ++n_epi;

@@ -71,6 +71,11 @@ def _bound(kv, mag, n, binades, d=0):
     ("mxfp4", 64, 2, 128, 32, 170, 1),
     ("mxfp4", 8, 1, 128, 16, 180, 3),
     ("mxfp4", 16, 1, 128, 16, 20000, 1),
+    ("fp8", 8, 2, 64, 16, 180, 1),
+    ("fp8", 16, 1, 128, 16, 4000, 1),
+    ("fp8", 8, 1, 128, 16, 180, 4),
+    ("fp8", 128, 1, 576, 64, 180, 1),
+    ("fp8", 128, 1, 576, 64, 4000, 2),
 ])
 def test_light_tokens_behind_an_empty_sink(kv, hq, hkv, d, bs, n, J, where):
     """A token 17.375 nats above all others holds a zero value: the output is the light tokens' share, 2^-25 each."""
