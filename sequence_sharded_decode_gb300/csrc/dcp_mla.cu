@@ -24,14 +24,9 @@
 // operand sit at the same shared-memory offsets in both CTAs, so a token half
 // of the page for the score and a value-dim half for P.V cannot share bytes,
 // and 128 heads fill only half of a pair MMA's 256 rows.) Both CTAs need
-// every page; the pair copies each page once: each CTA fetches alternate
-// 64-column boxes and the copy (TMA multicast) lands in both CTAs, so a
-// stage is free again only when both CTAs' P.V of its page finished. CTA 0
-// also pulls each page into L2 four pages ahead. Measured against each CTA
-// copying the whole page itself: +5.8 % on the 512-sequence workload (half
-// the L2 reads; it no longer runs into the power cap), -2 to -3 % on MLA long
-// and MLA decode (the coupled stage release). Per 64-token tile (= one paged
-// block):
+// every page, and each copies it itself, a stage being free again when its own
+// P.V of the page finished; CTA 0 also pulls each page into L2 four pages
+// ahead. Per 64-token tile (= one paged block):
 //   1. S = Q . K^T (M=128 heads, N=64 tokens, K=576) into TMEM; query dims
 //      0-383 are the MMA's A operand in TMEM, dims 384-575 in shared memory
 //   2. online softmax per head row, in log2 units, lazy rescale of O (only
@@ -401,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kRing; ++s) {
       bar_init(bar(BKV_FULL + s), 1);
       // bf16: the P.V of both CTAs (the page lands in both); F8: the widening of the codes
-      bar_init(bar(BKV_EMPTY + s), F8 ? kSoftmaxThreads + 1 : 2);  // F8: + the producer's rope box
+      bar_init(bar(BKV_EMPTY + s), F8 ? kSoftmaxThreads + 1 : 1);  // F8: + the producer's rope box
     }
     for (int q4 = 0; q4 < 4; ++q4) bar_init(bar(BXCH + q4), 64);  // the two warps of a lane quadrant
     bar_init(bar(BF_FULL), kSoftmaxThreads + 1);  // the softmax threads and the producer (rope box)
@@ -489,13 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             } else {
               const int row = phys < 0 ? -kTile : phys * kTile;  // out of range: the copy reads zeros
-              // the pair copies each page once: each CTA fetches alternate boxes
-              // into both CTAs (one L2 read per box); every CTA's barrier
-              // expects the whole page
               bar_arrive_tx(bar(BKV_FULL + s), kChunks * kKvChunkBytes);
-              for (int c = (int)rank; c < kChunks; c += 2)
-                tma_load_mc(sbase + kOffKv + s * kStageBytes + c * kKvChunkBytes, &p.tm_kv[g.shard], 64 * c, row,
-                            bar(BKV_FULL + s), 0x3);
+              for (int c = 0; c < kChunks; ++c)
+                tma_load(sbase + kOffKv + s * kStageBytes + c * kKvChunkBytes, &p.tm_kv[g.shard], 64 * c, row,
+                         bar(BKV_FULL + s));
             }
             if (kPrefetch > 0 && rank == 0 && phys_pf >= 0)
               l2_prefetch(static_cast<const char*>(p.sh.k[g.shard]) + (size_t)phys_pf * kStage, kStage);
@@ -543,11 +535,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0 && *abort_flag) {  // copies in flight must land before the CTA may exit
       if (!F8 && q_done > 0) drain_bar(bar(BQT), (q_done - 1) & 1u);
-      // (the other CTA's copies into this one land on the same barriers; it
-      // can be at most one page ahead, which may never complete here: the
-      // poll bound ends that wait)
+      // (F8 may have left with a page copied and not counted yet; where there
+      // is none, the poll bound ends that wait)
       const uint32_t f0 = fills > (uint32_t)kRing ? fills - kRing : 0;
-      for (uint32_t f = f0; f < fills + 1; ++f) drain_bar(bar(BKV_FULL + f % kRing), (f / kRing) & 1u);
+      for (uint32_t f = f0; f < fills + (F8 ? 1 : 0); ++f) drain_bar(bar(BKV_FULL + f % kRing), (f / kRing) & 1u);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ score MMA issuer
@@ -670,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               mma_ss(tmem + kColO, pd + (uint64_t)((term * kPBytes + 32 * kt) >> 4),
                   vd + (uint64_t)((2048 * kt) >> 4), id_pv, (jp == 0 && !acc_in && term == 0 && kt == 0) ? 0 : 1);
           }
-          if (!F8) mma_commit_mc(bar(BKV_EMPTY + s), 0x3);  // the stage is free in both CTAs once both P.V finished
+          if (!F8) mma_commit(bar(BKV_EMPTY + s));  // the stage is free once its P.V finished
           // (F8: the value slot and P may be overwritten)
           mma_commit(bar(BP_EMPTY + s));  // also tells softmax that this P.V finished
           if (++jp == ntp) {
@@ -1178,10 +1169,12 @@ __global__ void __launch_bounds__(kFinishThreads) mla_finish_kernel(const char* 
 // tcgen05 MMA of M = 128, K = 16 takes ~37 cycles for any N up to 64, so 36
 // MMAs of N = 32 cost about what 36 of N = 64 do; the gain is the deeper
 // pipeline.) Per page and CTA:
-//   1. the copies (three TMA copies): its own tokens' other value dims, which
-//      the other CTA needs for P.V (one multicast copy into both CTAs, at
-//      the same slots), its own tokens' value dims, dims 512-575; plus the
-//      other CTA's multicast of its tokens' rows of this CTA's value dims
+//   1. the copies (four TMA copies): its own tokens' other value dims (for the
+//      score), the other tokens' rows of its own value dims (for P.V), its own
+//      tokens' value dims, dims 512-575. (Copying the first two once for both
+//      CTAs would save 4 of 13 boxes of L2 reads: 0.488 against 0.498 ms on MLA
+//      long, 11.75 against 12.06 ms on the 512-sequence step. Not done: programs
+//      that use several GPUs may load this library.)
 //   2. S_r into TMEM (query dims 0-447 as the A operand in TMEM, 448-575 in
 //      shared memory)
 //   3. the row maximum of the own 32 tokens, sent to the other CTA (st.async
@@ -1208,9 +1201,10 @@ constexpr int kHalf = 32;                          // tokens of a page per CTA
 constexpr int kBox = kHalf * 128;                  // 64 columns x 32 rows of bf16: 4 KB
 constexpr int kSlots = 14;                         // boxes per stage
 constexpr int kStage = kSlots * kBox;              // 56 KB
-// slots of a stage: 0-3 tokens 0-31 x dims 256-511 (copied by CTA 0 into
-// both), 4-7 tokens 32-63 x dims 0-255 (copied by CTA 1 into both), 8-11 the
-// own tokens x the own value dims, 12 the own tokens x dims 512-575, 13 spare.
+// slots of a stage: 0-3 tokens 0-31 x dims 256-511, 4-7 tokens 32-63 x dims
+// 0-255 (of these two, CTA r's score reads 4r .. 4r + 3 and its P.V the others),
+// 8-11 the own tokens x the own value dims, 12 the own tokens x dims 512-575, 13
+// spare.
 // After the score, CTA r's slots 4r .. 4r + 3 hold P_hi (two token halves of
 // 8 KB: its own and the other CTA's) and slots 12-13 its own P_lo.
 constexpr int kSlotOwnV = 8, kSlotRope = 12, kSlotLo = 12;
@@ -1259,13 +1253,6 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_load4_mc(uint32_t dst, const CUtensorMap* map, int y, int z, uint32_t bar,
-                                             uint16_t cta_mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "h"(cta_mask) : "memory");
 }
 // the same shared-memory offset in CTA `peer` of the cluster
 __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t peer) {
@@ -1442,11 +1429,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // rows of this CTA's tokens (an unusable entry reads zeros above row 0)
             const int row = (phys < 0 ? -kTile : phys * kTile) + kHalf * (int)rank;
             const uint32_t st = stage_base(s);
-            // 13 boxes land here: 5 private, 4 of this CTA's multicast, 4 of the other's
             bar_arrive_tx(bar(B_KVFULL + s), 13 * kBox);
-            // the other CTA's value dims of the own tokens (into both CTAs), the
-            // own value dims, dims 512-575
-            tma_load4_mc(st + 4 * rank * kBox, &p.tm_kv4[g.shard], row, 4 * (int)peer, bar(B_KVFULL + s), 0x3);
+            // the own tokens' other value dims, the other tokens' own value dims
+            // (in the other half page), the own tokens' own value dims, dims 512-575
+            tma_load4(st + 4 * rank * kBox, &p.tm_kv4[g.shard], row, 4 * (int)peer, bar(B_KVFULL + s));
+            tma_load4(st + 4 * peer * kBox, &p.tm_kv4[g.shard], row + kHalf * ((int)peer - (int)rank), 4 * (int)rank,
+                      bar(B_KVFULL + s));
             tma_load4(st + kSlotOwnV * kBox, &p.tm_kv4[g.shard], row, 4 * (int)rank, bar(B_KVFULL + s));
             tma_load(st + kSlotRope * kBox, &p.tm_kv[g.shard], 512, row, bar(B_KVFULL + s));
             if (kPrefetch > 0 && rank == 0 && phys_pf >= 0)
@@ -1460,7 +1448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0 && *abort_flag) {  // copies in flight must land before the CTA may exit
       if (q_done > 0) drain_bar(bar(B_QT), (q_done - 1) & 1u);
       const uint32_t f0 = fills > (uint32_t)kStages ? fills - kStages : 0;
-      for (uint32_t f = f0; f < fills + 1; ++f) drain_bar(bar(B_KVFULL + f % kStages), (f / kStages) & 1u);
+      for (uint32_t f = f0; f < fills; ++f) drain_bar(bar(B_KVFULL + f % kStages), (f / kStages) & 1u);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ score MMA issuer

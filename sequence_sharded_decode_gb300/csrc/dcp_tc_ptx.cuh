@@ -103,16 +103,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-// The same tile copy delivered to the same shared-memory offset of every CTA
-// of the cluster in cta_mask, each of whose mbarriers at offset `bar`
-// receives the bytes that land in that CTA.
-__device__ __forceinline__ void tma_load_mc(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                            uint16_t cta_mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;\n"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(cta_mask) : "memory");
-}
 // All threads of every CTA of the cluster meet here (release / acquire).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
