@@ -79,6 +79,8 @@ class DecodeState:
         self.o = torch.empty((*rows, wl.q_heads, wl.dv), dtype=torch.float32, device=device)
         self.lse = torch.empty((*rows, wl.q_heads), dtype=torch.float32, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.steps_taken = 0        # after the first one
+        self.between_steps = False  # after an eviction, until the next step's tokens are appended
         if fill:
             self.fill_context(fill_chunk)
 
@@ -119,10 +121,20 @@ class DecodeState:
 
     # -- the decode step through the C ABI ------------------------------------
     def append(self, stream=None):
+        """The step's tokens into the cache; after an eviction those of the next
+        step (advance())."""
+        if self.between_steps:
+            self.advance(stream)
         dcp.dcp_kv_append(self.desc, self.shards, self.starts, self.positions, self.k_new, self.v_new,
                           seq_ids=self.seq_ids, err=self.err, stream=stream)
 
+    def _check_appended(self):
+        # several query tokens see each other causally, as the last q_len cached tokens
+        if self.between_steps and self.q_len > 1:
+            raise RuntimeError("after an eviction, append the next step's tokens first")
+
     def partial(self, stream=None):
+        self._check_appended()
         if self.q_len == 1:
             dcp.dcp_decode_partial_all(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.o_parts,
                                        self.lses, self.workspace, err=self.err, stream=stream)
@@ -132,6 +144,7 @@ class DecodeState:
 
     def attention(self, stream=None):
         """Partial attention of every shard and the merge in one call."""
+        self._check_appended()
         dcp.dcp_attention_all(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.o_parts, self.lses,
                               self.o, self.lse, self.workspace, err=self.err, stream=stream)
 
@@ -142,19 +155,26 @@ class DecodeState:
     def weigh(self, stream=None):
         """Add the attention weight that this step gave every cached token (after
         attention() or partial() and merge(), whose LSE it takes)."""
+        self._check_appended()
         if not hasattr(self, "mass"):
-            wl = self.wl
-            cap = int(self.ctx.max()) + self.q_len if wl.batch else 1
-            self.mass = torch.zeros((wl.batch, wl.kv_heads, cap), dtype=torch.float32, device=self.device)
+            cap = int(self.ctx.max()) + self.q_len if self.wl.batch else 1
+            self.mass = torch.zeros((self.wl.batch, self.wl.kv_heads, cap), dtype=torch.float32, device=self.device)
             self.pos = self.known_lens = None
-            self.total_lens = self.seq_lens
+            self.total_lens = self.seq_lens.clone()
+        if self.between_steps:  # none of the cached tokens is the step's own, whose weight would start at 0
+            here = torch.zeros_like(self.mass)
+            dcp.dcp_attention_mass(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.lse, here,
+                                   err=self.err, stream=stream)
+            self.mass += here
+            return
         dcp.dcp_attention_mass(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.lse, self.mass,
                                mass_in=self.mass, err=self.err, stream=stream)
 
     def evict(self, keep: torch.Tensor, n_sink: int = 4, n_recent: int = 32, stream=None):
         """Keep the keep[b, i] (int32 [B, N]) heaviest tokens of every shard and
-        KV head; the state goes on with the shortened sequences. total_lens (the
-        text's length, which fixes the positions of later tokens) stays."""
+        KV head. The state goes on with the shortened sequences: the next
+        append() brings the next step's tokens. (A state of one query token may
+        attend and weigh the kept ones again before that.)"""
         wl = self.wl
         cap = self.mass.shape[-1]
         if not hasattr(self, "evict_workspace"):
@@ -166,6 +186,25 @@ class DecodeState:
                          pos, starts, lens, self.evict_workspace, pos_in=self.pos, known_lens=self.known_lens,
                          total_lens=self.total_lens, err=self.err, stream=stream)
         self.mass, self.pos, self.starts, self.seq_lens, self.known_lens = mass, pos, starts, lens, lens
+        self.between_steps = True
+
+    def advance(self, stream=None):
+        """On to the next step after an eviction (append() does it): its tokens
+        follow the kept ones in the cache, at index seq_lens of the last shard,
+        whose freed blocks take them, and the evicted ones too in the text, where
+        total_lens counts. One that finds no room raises the error flag."""
+        if not self.between_steps:
+            raise RuntimeError("the step's tokens are the state's last ones already")
+        B, J = self.wl.batch, self.q_len
+        text = (self.ctx + J * (self.steps_taken + 1)).repeat(J) + np.tile(np.arange(J), B)
+        k, v = self.token_rows(np.repeat(np.arange(B), J), text)
+        new = torch.arange(J, dtype=torch.int32, device=self.device)
+        self.k_new, self.v_new = k, v
+        self.positions = (self.known_lens[:, None] + new).reshape(-1)
+        self.seq_lens = self.known_lens + J
+        self.total_lens = self.total_lens + J
+        self.steps_taken += 1
+        self.between_steps = False
 
     def step(self, stream=None, fused: bool = False):
         """append -> partial attention of every shard -> merge; fused: the last
@@ -180,16 +219,23 @@ class DecodeState:
             self.merge(stream)
 
     # -- algorithmic bytes ---------------------------------------------------
+    def _cached(self) -> np.ndarray:
+        """Tokens cached before the step, per sequence (after an eviction they are
+        read from the device)."""
+        if not self.steps_taken and not self.between_steps:
+            return self.ctx
+        return self.seq_lens.cpu().numpy().astype(np.int64) - self.q_len
+
     def attended_tokens(self) -> int:
         """Distinct tokens the step attends: the context plus the new tokens
         (with several query tokens, each token is still read from HBM once)."""
-        return int((self.ctx + self.q_len).sum())
+        return int((self._cached() + self.q_len).sum())
 
     def attention_flops(self) -> int:
         """Multiply-add flops of the partial pass: for every query token, q.k
         and p.v over each token it attends (2 (Dk + Dv) per head and token)."""
         wl = self.wl
-        per_seq = self.q_len * (self.ctx + 1) + self.q_len * (self.q_len - 1) // 2  # sum_j (ctx + j + 1)
+        per_seq = self.q_len * (self._cached() + 1) + self.q_len * (self.q_len - 1) // 2  # sum_j (ctx + j + 1)
         return int(2 * wl.q_heads * (wl.dk + wl.dv) * per_seq.sum())
 
     def kv_bytes(self) -> int:
