@@ -8,10 +8,30 @@ add the eviction of the cached tokens with the least attention weight.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
 from . import configs, dcp, inputs
+
+
+def _on(stream):
+    """Context in which torch's own work and memory belong to `stream` (a
+    torch stream, a handle, or None for the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _release(*tensors):
+    """Before tensors are dropped: their memory, of whichever stream, is kept
+    until the current stream has run what reads them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream())
 
 
 class DecodeState:
@@ -156,19 +176,18 @@ class DecodeState:
         """Add the attention weight that this step gave every cached token (after
         attention() or partial() and merge(), whose LSE it takes)."""
         self._check_appended()
-        if not hasattr(self, "mass"):
-            cap = int(self.ctx.max()) + self.q_len if self.wl.batch else 1
-            self.mass = torch.zeros((self.wl.batch, self.wl.kv_heads, cap), dtype=torch.float32, device=self.device)
-            self.pos = self.known_lens = None
-            self.total_lens = self.seq_lens.clone()
-        if self.between_steps:  # none of the cached tokens is the step's own, whose weight would start at 0
-            here = torch.zeros_like(self.mass)
+        with _on(stream):
+            if not hasattr(self, "mass"):
+                cap = int(self.ctx.max()) + self.q_len if self.wl.batch else 1
+                self.mass = torch.zeros((self.wl.batch, self.wl.kv_heads, cap), dtype=torch.float32, device=self.device)
+                self.pos = self.known_lens = None
+                self.total_lens = self.seq_lens.clone()
+            # right after an eviction none of the cached tokens is the step's own, whose weight would start at 0
+            here = torch.zeros_like(self.mass) if self.between_steps else self.mass
             dcp.dcp_attention_mass(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.lse, here,
-                                   err=self.err, stream=stream)
-            self.mass += here
-            return
-        dcp.dcp_attention_mass(self.desc, self.q, self.shards, self.seq_lens, self.starts, self.lse, self.mass,
-                               mass_in=self.mass, err=self.err, stream=stream)
+                                   mass_in=None if self.between_steps else here, err=self.err)
+            if self.between_steps:
+                self.mass += here
 
     def evict(self, keep: torch.Tensor, n_sink: int = 4, n_recent: int = 32, stream=None):
         """Keep the keep[b, i] (int32 [B, N]) heaviest tokens of every shard and
@@ -177,14 +196,16 @@ class DecodeState:
         attend and weigh the kept ones again before that.)"""
         wl = self.wl
         cap = self.mass.shape[-1]
-        if not hasattr(self, "evict_workspace"):
-            size = dcp.dcp_evict_workspace_size(self.desc, wl.batch, wl.shards, cap)
-            self.evict_workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-        mass, pos = torch.zeros_like(self.mass), torch.zeros(self.mass.shape, dtype=torch.int32, device=self.device)
-        starts, lens = torch.empty_like(self.starts), torch.empty_like(self.seq_lens)
-        dcp.dcp_kv_evict(self.desc, self.shards, self.seq_lens, self.starts, keep, n_sink, n_recent, self.mass, mass,
-                         pos, starts, lens, self.evict_workspace, pos_in=self.pos, known_lens=self.known_lens,
-                         total_lens=self.total_lens, err=self.err, stream=stream)
+        with _on(stream):
+            if not hasattr(self, "evict_workspace"):
+                size = dcp.dcp_evict_workspace_size(self.desc, wl.batch, wl.shards, cap)
+                self.evict_workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+            mass, pos = torch.zeros_like(self.mass), torch.zeros(self.mass.shape, dtype=torch.int32, device=self.device)
+            starts, lens = torch.empty_like(self.starts), torch.empty_like(self.seq_lens)
+            dcp.dcp_kv_evict(self.desc, self.shards, self.seq_lens, self.starts, keep, n_sink, n_recent, self.mass,
+                             mass, pos, starts, lens, self.evict_workspace, pos_in=self.pos,
+                             known_lens=self.known_lens, total_lens=self.total_lens, err=self.err)
+            _release(keep, self.mass, self.pos, self.starts, self.seq_lens, self.known_lens)
         self.mass, self.pos, self.starts, self.seq_lens, self.known_lens = mass, pos, starts, lens, lens
         self.between_steps = True
 
@@ -197,12 +218,14 @@ class DecodeState:
             raise RuntimeError("the step's tokens are the state's last ones already")
         B, J = self.wl.batch, self.q_len
         text = (self.ctx + J * (self.steps_taken + 1)).repeat(J) + np.tile(np.arange(J), B)
-        k, v = self.token_rows(np.repeat(np.arange(B), J), text)
-        new = torch.arange(J, dtype=torch.int32, device=self.device)
-        self.k_new, self.v_new = k, v
-        self.positions = (self.known_lens[:, None] + new).reshape(-1)
-        self.seq_lens = self.known_lens + J
-        self.total_lens = self.total_lens + J
+        with _on(stream):
+            k, v = self.token_rows(np.repeat(np.arange(B), J), text)
+            _release(self.k_new, self.v_new, self.positions, self.seq_lens, self.total_lens)
+            self.k_new, self.v_new = k, v
+            new = torch.arange(J, dtype=torch.int32, device=self.device)
+            self.positions = (self.known_lens[:, None] + new).reshape(-1)
+            self.seq_lens = self.known_lens + J
+            self.total_lens = self.total_lens + J
         self.steps_taken += 1
         self.between_steps = False
 

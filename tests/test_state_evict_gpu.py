@@ -141,3 +141,56 @@ def test_evictions_in_a_row():
     st.step(fused=True)
     torch.cuda.synchronize()
     assert st.seq_lens.tolist() == [21, 21] and int(st.err.item()) == 0
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Work on the current stream is not waited for and does not reach into the calls on another one."""
+    keep = torch.full((2, 2), 40, dtype=torch.int32, device="cuda")
+    want = _state("bf16")
+    want.step(fused=True)
+    want.weigh()
+    want.evict(keep)
+    want.step(fused=True)
+    want.weigh()
+    torch.cuda.synchronize()
+    st = _state("bf16")
+    st.step(fused=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)                        # ~50 ms, on the current stream
+    st.weigh(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    st.evict(keep, stream=side.cuda_stream)
+    st.step(stream=side, fused=True)
+    st.weigh(stream=side.cuda_stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(st.seq_lens, want.seq_lens) and torch.equal(st.pos[:, :, :80], want.pos[:, :, :80])
+    assert torch.equal(st.mass[:, :, :81], want.mass[:, :, :81]) and torch.equal(st.o, want.o)
+    assert int(st.err.item()) == 0
+
+
+def test_memory_let_go_is_not_reused_under_a_waiting_call():
+    """Tensors that an eviction on a busy stream replaces stay as they are until it has run, whatever the current stream
+    allocates meanwhile."""
+    keep = torch.full((2, 2), 40, dtype=torch.int32, device="cuda")
+    results = []
+    for wait in (False, True):
+        st = _state("bf16", ctx=2000)
+        st.step(fused=True)
+        st.weigh()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            if wait:
+                torch.cuda._sleep(200_000_000)            # ~100 ms
+        sizes = [st.mass.numel(), st.starts.numel(), st.seq_lens.numel()]
+        st.evict(keep, stream=side)
+        st.step(stream=side, fused=True)
+        junk = [torch.full((n,), 3, dtype=torch.int32, device="cuda") for n in sizes * 20]  # on the current stream
+        torch.cuda.synchronize()
+        results.append((st.mass[:, :, :80].clone(), st.pos[:, :, :80].clone(), st.o.clone()))
+        assert int(st.err.item()) == 0 and len(junk) == 60
+    assert all(torch.equal(a, b) for a, b in zip(*results))
