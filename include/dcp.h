@@ -405,7 +405,8 @@ DCP_API int dcp_merge(const float* o_parts, const float* lses, int N, int B, int
  *   mass_in   device fp32 [B, num_kv_heads, max_tokens], or NULL (all zero);
  *             may be mass_out (in place)
  *   mass_out  device fp32 [B, num_kv_heads, max_tokens] (out); entries at or
- *             past seq_lens[b] are left as they were
+ *             past seq_lens[b] are left as they were; shares no memory with
+ *             the other arguments
  * A sequence longer than max_tokens raises DCP_DEVERR_TABLE_RANGE and its
  * tokens past max_tokens are left out. No workspace; the result does not
  * depend on the order of the work. shard_starts of a sequence may not fall
@@ -451,7 +452,8 @@ DCP_API size_t dcp_evict_workspace_size(const dcp_attn_desc* desc, int B, int N,
  *               index; entries at or past new_lens[b] are left as they were
  *   new_starts  device int32 [B, N] (out): sum of the k of the shards before i
  *   new_lens    device int32 [B] (out): sum of k over the shards
- * Outputs may not be the inputs. A sequence longer than max_tokens raises
+ * The outputs and the workspace share no memory with each other or with the
+ * inputs (DCP_ERR_INVALID_ARG). A sequence longer than max_tokens raises
  * DCP_DEVERR_TABLE_RANGE and its tokens past max_tokens are dropped; a move
  * through a bad table entry raises the flag and is skipped. The call is
  * repeatable: with the same inputs it makes the same copies again.

@@ -125,6 +125,17 @@ static Path path_for(const dcp_attn_desc& d, int q_len) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Bytes that an argument takes up; do two share any? (a NULL one: none)
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+
 static int check_desc(const dcp_attn_desc* d) {
   if (!d) return DCP_ERR_INVALID_ARG;
   if (d->kind != DCP_KIND_GQA && d->kind != DCP_KIND_MLA) return DCP_ERR_INVALID_ARG;
@@ -354,6 +365,17 @@ int dcp_attention_mass(const dcp_attn_desc* desc, const void* q, const dcp_shard
   if (!q || !seq_lens || !shard_starts || !lse || !mass_out) return DCP_ERR_INVALID_ARG;
   if (!aligned16(q)) return DCP_ERR_INVALID_ARG;
   if ((long long)B * q_len > INT32_MAX || (long long)B * N > (1 << 22)) return DCP_ERR_SHAPE;
+  {
+    const size_t rows = (size_t)B * desc->num_kv_heads;  // (bytes of the masses, as many as there can be)
+    const size_t mass = (size_t)max_tokens > SIZE_MAX / 4 / rows ? SIZE_MAX : rows * (size_t)max_tokens * 4;
+    const Range in[] = {{q, (size_t)B * q_len * desc->num_q_heads * desc->head_dim_k * 2},
+                        {lse, (size_t)B * q_len * desc->num_q_heads * 4},
+                        {seq_lens, (size_t)B * 4},
+                        {shard_starts, (size_t)B * N * 4},
+                        {mass_in == mass_out ? nullptr : mass_in, mass}};  // (in place is fine)
+    for (const Range& r : in)
+      if (overlap({mass_out, mass}, r)) return DCP_ERR_INVALID_ARG;
+  }
   const cudaError_t e = launch_mass(*desc, sh, N, q, seq_lens, shard_starts, B, q_len, lse, mass_in, mass_out, max_tokens,
                                     dev_err_flag, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return DCP_ERR_UNSUPPORTED;
@@ -382,13 +404,24 @@ int dcp_kv_evict(const dcp_attn_desc* desc, const dcp_shard* shards, int N, cons
     return DCP_ERR_INVALID_ARG;
   if (!pos_in != !known_lens) return DCP_ERR_INVALID_ARG;
   // the outputs are written while the inputs are still read
-  if (mass_in == mass_out || pos_in == pos_out || shard_starts == new_starts || seq_lens == new_lens ||
-      known_lens == new_lens || total_lens == new_lens)
-    return DCP_ERR_INVALID_ARG;
+  const void* const in[] = {seq_lens, shard_starts, keep, mass_in, pos_in, known_lens, total_lens};
+  const void* const out[] = {mass_out, pos_out, new_starts, new_lens};
+  for (const void* o : out)
+    for (const void* i : in)
+      if (o == i) return DCP_ERR_INVALID_ARG;
   if (max_tokens > INT32_MAX || (long long)B * N * desc->num_kv_heads > (1 << 22)) return DCP_ERR_SHAPE;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       ws_bytes < evict_workspace(*desc, B, N, max_tokens))
     return DCP_ERR_WORKSPACE;
+  {
+    const size_t lens = (size_t)B * 4, table = lens * N, rows = lens * desc->num_kv_heads * (size_t)max_tokens;
+    const Range mem[] = {{mass_out, rows},     {pos_out, rows}, {new_starts, table}, {new_lens, lens},
+                         {workspace, ws_bytes}, {seq_lens, lens}, {shard_starts, table}, {keep, table},
+                         {mass_in, rows},      {pos_in, rows},  {known_lens, lens},  {total_lens, lens}};
+    for (int o = 0; o < 5; ++o)  // the outputs and the workspace, with all that follow
+      for (int i = o + 1; i < 12; ++i)
+        if (overlap(mem[o], mem[i])) return DCP_ERR_INVALID_ARG;
+  }
   if (launch_evict(*desc, sh, N, seq_lens, shard_starts, B, keep, n_sink, n_recent, mass_in, pos_in, known_lens,
                    total_lens, max_tokens, mass_out, pos_out, new_starts, new_lens, workspace, dev_err_flag,
                    static_cast<cudaStream_t>(stream)) != cudaSuccess)
