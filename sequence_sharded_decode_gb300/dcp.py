@@ -80,10 +80,11 @@ class AttnDesc:
     v_scale: float = 1.0
 
     def c(self) -> _Desc:
-        return self._c
+        """The descriptor's library form, the caller's own."""
+        return _Desc.from_buffer_copy(self._c)
 
     @functools.cached_property
-    def _c(self) -> _Desc:  # (the fields are frozen, and the library only reads it)
+    def _c(self) -> _Desc:  # the calls' (the fields are frozen, and the library only reads it)
         return _Desc(self.kind, self.num_q_heads, self.num_kv_heads, self.head_dim_k, self.head_dim_v,
                      self.block_size, self.scale, self.kv_dtype, self.k_scale, self.v_scale)
 
@@ -118,8 +119,8 @@ class Shard:
     """One shard's pool(s) and block table (device tensors).
 
     The tensors are checked and their library form is made when the shard is
-    first used, and again after a field is set or a tensor's storage or shape
-    changes."""
+    first used, and again after a field is set or a tensor's storage, shape,
+    type or order changes."""
     k_pool: torch.Tensor
     v_pool: torch.Tensor | None
     block_table: torch.Tensor
@@ -128,14 +129,22 @@ class Shard:
         self.__dict__[name] = value
         self.__dict__["_made"] = None
 
+    def __getstate__(self):
+        return {"k_pool": self.k_pool, "v_pool": self.v_pool, "block_table": self.block_table}
+
+    def __setstate__(self, state):
+        for name, value in state.items():
+            setattr(self, name, value)
+
     def c(self) -> _Shard:
-        return self._form()[0]
+        """The shard's library form, the caller's own."""
+        return _Shard.from_buffer_copy(self._form()[0])
 
     def _form(self):
-        """(library form, pointers and shapes, (device, pool type, table rows, elements of a key and a value block))"""
+        """(library form, what it was made of, (device, pool type, table rows, elements of a key and a value block))"""
         made, k, v, t = self._made, self.k_pool, self.v_pool, self.block_table
-        now = (k.data_ptr(), None if v is None else v.data_ptr(), t.data_ptr(), k.shape, None if v is None else v.shape,
-               t.shape)
+        now = (k.data_ptr(), None if v is None else v.data_ptr(), t.data_ptr(), k.shape, t.shape, k.dtype, t.dtype,
+               k.is_contiguous(), t.is_contiguous(), v is None or (v.shape, v.dtype, v.is_contiguous()))
         if made is not None and made[1] == now:
             return made
         if k.dtype not in (torch.bfloat16, torch.uint8):
@@ -240,7 +249,7 @@ def _shards(shards) -> ctypes.Array:
     n = len(shards)
     arr = (_SHARD_ARRAYS[n] if n <= DCP_MAX_SHARDS else _Shard * n)()
     for i, s in enumerate(shards):
-        arr[i] = s.c()
+        arr[i] = s._form()[0]
     return arr
 
 
@@ -287,18 +296,18 @@ def dcp_kv_append(desc: AttnDesc, shards, shard_starts: torch.Tensor, positions:
     B = int(shard_starts.shape[0])
     T = int(positions.numel())
     arr = _shards(shards)
-    rc = load().dcp_kv_append(ctypes.byref(desc.c()), arr, len(shards), shard_starts.data_ptr(), B,
+    rc = load().dcp_kv_append(ctypes.byref(desc._c), arr, len(shards), shard_starts.data_ptr(), B,
                               _ptr(seq_ids), positions.data_ptr(), k_new.data_ptr(), _ptr(v_new), T,
                               _ptr(err), _stream(stream))
     _raise(rc, "dcp_kv_append")
 
 
 def dcp_workspace_size(desc: AttnDesc, batch: int, n_shards: int) -> int:
-    return int(load().dcp_workspace_size(ctypes.byref(desc.c()), batch, n_shards))
+    return int(load().dcp_workspace_size(ctypes.byref(desc._c), batch, n_shards))
 
 
 def dcp_workspace_size_mtp(desc: AttnDesc, batch: int, q_len: int, n_shards: int) -> int:
-    return int(load().dcp_workspace_size_mtp(ctypes.byref(desc.c()), batch, q_len, n_shards))
+    return int(load().dcp_workspace_size_mtp(ctypes.byref(desc._c), batch, q_len, n_shards))
 
 
 def dcp_decode_partial(desc: AttnDesc, q: torch.Tensor, shard: Shard, seq_lens: torch.Tensor,
@@ -313,7 +322,7 @@ def dcp_decode_partial(desc: AttnDesc, q: torch.Tensor, shard: Shard, seq_lens: 
     if err is not None:
         _check(err, torch.int32, "err")
     arr = _shards([shard])
-    rc = load().dcp_decode_partial(ctypes.byref(desc.c()), q.data_ptr(), arr, seq_lens.data_ptr(),
+    rc = load().dcp_decode_partial(ctypes.byref(desc._c), q.data_ptr(), arr, seq_lens.data_ptr(),
                                    shard_range.data_ptr(), int(q.shape[0]), o_part.data_ptr(), lse.data_ptr(),
                                    workspace.data_ptr(), workspace.numel(), _ptr(err), _stream(stream))
     _raise(rc, "dcp_decode_partial")
@@ -331,7 +340,7 @@ def dcp_decode_partial_all(desc: AttnDesc, q: torch.Tensor, shards, seq_lens: to
     if err is not None:
         _check(err, torch.int32, "err")
     arr = _shards(shards)
-    rc = load().dcp_decode_partial_all(ctypes.byref(desc.c()), q.data_ptr(), arr, len(shards),
+    rc = load().dcp_decode_partial_all(ctypes.byref(desc._c), q.data_ptr(), arr, len(shards),
                                        seq_lens.data_ptr(), shard_starts.data_ptr(), int(q.shape[0]),
                                        o_parts.data_ptr(), lses.data_ptr(), workspace.data_ptr(),
                                        workspace.numel(), _ptr(err), _stream(stream))
@@ -356,7 +365,7 @@ def dcp_decode_partial_all_mtp(desc: AttnDesc, q: torch.Tensor, shards, seq_lens
     if q.dim() != 4:
         raise ValueError("q must be [B, q_len, Hq, Dk]")
     arr = _shards(shards)
-    rc = load().dcp_decode_partial_all_mtp(ctypes.byref(desc.c()), q.data_ptr(), arr, len(shards),
+    rc = load().dcp_decode_partial_all_mtp(ctypes.byref(desc._c), q.data_ptr(), arr, len(shards),
                                            seq_lens.data_ptr(), shard_starts.data_ptr(), int(q.shape[0]),
                                            int(q.shape[1]), o_parts.data_ptr(), lses.data_ptr(),
                                            workspace.data_ptr(), workspace.numel(), _ptr(err), _stream(stream))
@@ -383,7 +392,7 @@ def dcp_attention_all(desc: AttnDesc, q: torch.Tensor, shards, seq_lens: torch.T
         _check(err, torch.int32, "err")
     q_len = 1 if q.dim() == 3 else int(q.shape[1])
     arr = _shards(shards)
-    rc = load().dcp_attention_all(ctypes.byref(desc.c()), q.data_ptr(), arr, len(shards), seq_lens.data_ptr(),
+    rc = load().dcp_attention_all(ctypes.byref(desc._c), q.data_ptr(), arr, len(shards), seq_lens.data_ptr(),
                                   shard_starts.data_ptr(), int(q.shape[0]), q_len, o_parts.data_ptr(),
                                   lses.data_ptr(), o.data_ptr(), _ptr(lse_out), workspace.data_ptr(),
                                   workspace.numel(), _ptr(err), _stream(stream))
@@ -403,7 +412,7 @@ def dcp_decode_partial_all_noalloc(desc: AttnDesc, q: torch.Tensor, shards, seq_
     if err is not None:
         _check(err, torch.int32, "err")
     arr = _shards(shards)
-    rc = load().dcp_decode_partial_all_noalloc(ctypes.byref(desc.c()), q.data_ptr(), arr, len(shards),
+    rc = load().dcp_decode_partial_all_noalloc(ctypes.byref(desc._c), q.data_ptr(), arr, len(shards),
                                                seq_lens.data_ptr(), shard_starts.data_ptr(), int(q.shape[0]),
                                                o_parts.data_ptr(), lses.data_ptr(), _ptr(err), _stream(stream))
     _raise(rc, "dcp_decode_partial_all_noalloc")
@@ -485,7 +494,7 @@ def dcp_kv_read(desc: AttnDesc, shards, shard_starts: torch.Tensor, positions: t
     if v_out is not None:
         _check_shape(v_out, torch.bfloat16, (T, desc.num_kv_heads, desc.head_dim_v), "v_out", dev)
     _check_err(err, dev)
-    rc = load().dcp_kv_read(ctypes.byref(desc.c()), arr, len(shards), shard_starts.data_ptr(), B,
+    rc = load().dcp_kv_read(ctypes.byref(desc._c), arr, len(shards), shard_starts.data_ptr(), B,
                             _ptr(seq_ids), positions.data_ptr(), k_out.data_ptr(), _ptr(v_out), T, _ptr(err),
                             _stream(stream))
     _raise(rc, "dcp_kv_read")
@@ -515,14 +524,14 @@ def dcp_attention_mass(desc: AttnDesc, q: torch.Tensor, shards, seq_lens: torch.
     if mass_in is not None:
         _check_shape(mass_in, torch.float32, (B, desc.num_kv_heads, cap), "mass_in", dev)
     _check_err(err, dev)
-    rc = load().dcp_attention_mass(ctypes.byref(desc.c()), q.data_ptr(), arr, len(shards),
+    rc = load().dcp_attention_mass(ctypes.byref(desc._c), q.data_ptr(), arr, len(shards),
                                    seq_lens.data_ptr(), shard_starts.data_ptr(), B, q_len, lse.data_ptr(),
                                    _ptr(mass_in), mass_out.data_ptr(), cap, _ptr(err), _stream(stream))
     _raise(rc, "dcp_attention_mass")
 
 
 def dcp_evict_workspace_size(desc: AttnDesc, batch: int, n_shards: int, max_tokens: int) -> int:
-    return int(load().dcp_evict_workspace_size(ctypes.byref(desc.c()), batch, n_shards, max_tokens))
+    return int(load().dcp_evict_workspace_size(ctypes.byref(desc._c), batch, n_shards, max_tokens))
 
 
 def dcp_kv_evict(desc: AttnDesc, shards, seq_lens: torch.Tensor, shard_starts: torch.Tensor, keep: torch.Tensor,
@@ -556,7 +565,7 @@ def dcp_kv_evict(desc: AttnDesc, shards, seq_lens: torch.Tensor, shard_starts: t
         _check_shape(total_lens, i32, (B,), "total_lens", dev)
     _check(workspace, torch.uint8, "workspace")
     _check_err(err, dev)
-    rc = load().dcp_kv_evict(ctypes.byref(desc.c()), arr, N, seq_lens.data_ptr(), shard_starts.data_ptr(),
+    rc = load().dcp_kv_evict(ctypes.byref(desc._c), arr, N, seq_lens.data_ptr(), shard_starts.data_ptr(),
                              B, keep.data_ptr(), n_sink, n_recent, mass_in.data_ptr(), _ptr(pos_in),
                              _ptr(known_lens), _ptr(total_lens), cap, mass_out.data_ptr(), pos_out.data_ptr(),
                              new_starts.data_ptr(), new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(),
