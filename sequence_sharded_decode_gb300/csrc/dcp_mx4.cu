@@ -293,6 +293,14 @@ __device__ __forceinline__ void read_key(const unsigned char* tile, int r, int l
   else reinterpret_cast<uint32_t*>(out)[lane] = w[0];
 }
 
+// A product for a further rounding: of the two fp32 values around it the odd one
+// (or itself), which no coarser format has a tie at, so that rounding it to bf16
+// rounds the exact product (28 bits) once.
+__device__ __forceinline__ float mul_odd(float a, float b) {
+  const float lo = __fmul_rd(a, b), hi = __fmul_ru(a, b);
+  return __float_as_uint(lo) & 1u ? lo : hi;
+}
+
 // Four E4M3 codes times a scale as four bf16 values.
 __device__ __forceinline__ uint2 e4m3_widen(uint32_t codes, float scale) {
   uint32_t h[2], v[2];
@@ -302,7 +310,7 @@ __device__ __forceinline__ uint2 e4m3_widen(uint32_t codes, float scale) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    const __nv_bfloat162 z = __floats2bfloat162_rn(scale * f.x, scale * f.y);
+    const __nv_bfloat162 z = __floats2bfloat162_rn(mul_odd(scale, f.x), mul_odd(scale, f.y));
     v[i] = *reinterpret_cast<const uint32_t*>(&z);
   }
   return make_uint2(v[0], v[1]);
@@ -313,8 +321,9 @@ __device__ __forceinline__ uint2 e4m3_widen(uint32_t codes, float scale) {
 // lanes, four in flight. 8-bit values lie transposed in their block: a lane each
 // token, whose neighbours' bytes lie beside its own. D 576: latent rows. 8 x 8192
 // tokens of 8 heads of 128 dims: bf16 93 us (79 of bytes; a warp per row 178),
-// 8-bit 165 us (59; 388), bound by the values' single bytes; latents 32 and 26 us
-// (22 and 17; 41 and 83).
+// 8-bit 169 us (59; 388), bound by the values' single bytes; latents 32 and 27 us
+// (22 and 17; 41 and 83). Products rounded twice would save 4 and 2 us of the
+// 8-bit ones.
 constexpr int rows_tokens(int d) { return d == 576 ? 8 : 32; }
 template <int KV, int D>
 __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_constant__ RowParams p) {
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
       const float scale = side ? p.v_scale : p.k_scale;
       const unsigned char* src = pool + blk * p.Bs * D;
       for (int d = lane; d < D; d += 32)
-        out[d] = __float2bfloat16(scale * e4m3_value(side ? src[(size_t)d * p.Bs + slot] : src[(size_t)slot * D + d]));
+        out[d] = __float2bfloat16(mul_odd(scale, e4m3_value(side ? src[(size_t)d * p.Bs + slot] : src[(size_t)slot * D + d])));
     } else {
       const unsigned char* t = mx4_tile(const_cast<unsigned char*>(pool), at.phys, p.Hkv, h, p.Bs, D, slot);
       const int r = slot % kMxTile;
