@@ -108,6 +108,13 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const __grid_constan
       uint32_t w[D / 64];
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) w[i] = valid ? reinterpret_cast<const uint32_t*>(p.q + qr * D)[lane + 32 * i] : 0u;
+      // a row that saw nothing weighs nothing, whatever it holds
+      const float l = valid ? p.lse[qr] : -INFINITY;
+      const bool some = l != -INFINITY;
+      if (!some) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) w[i] = 0u;
+      }
       int f = 127;
       if constexpr (KV != 0) {  // fp16 operands: the row's largest value into [1, 2)
         uint32_t top = 0;
@@ -128,8 +135,6 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const __grid_constan
         *reinterpret_cast<uint32_t*>(smem + r * kRowBytes + (lane + 32 * i) * 4) = w[i];
       }
       if (lane == 0) {
-        const float l = valid ? p.lse[qr] : -INFINITY;
-        const bool some = l != -INFINITY;  // a row that saw nothing weighs nothing
         row_scale[r] = some ? p.sl2 * __uint_as_float((uint32_t)f << 23) : 0.f;
         row_lse[r] = some ? l * kLog2e : INFINITY;
         row_lim[r] = valid ? len - (p.qlen - 1 - j) : INT_MIN;

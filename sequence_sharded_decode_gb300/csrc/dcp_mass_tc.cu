@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(MassTc<KV, D>::kThreads, D == 576 ? 1 : 2)
   __shared__ RunPlace place;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_word;
+  __shared__ volatile uint32_t left_out;  // the last part, from 1, with a row that weighs nothing
   const uint32_t raw = saddr(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t qbase = saddr(smem);
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(MassTc<KV, D>::kThreads, D == 576 ? 1 : 2)
     bar_init(bar(BQT), 1);        // the copies of them
     bar_init(bar(BDRAIN), 1);
     abort_word = 0;
+    left_out = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -400,12 +402,15 @@ __global__ void __launch_bounds__(MassTc<KV, D>::kThreads, D == 576 ? 1 : 2)
         const int row = r0 + r, j = row / p.g;
         float l = -INFINITY;
         if (r < here) l = p.lse[((size_t)b * p.qlen + j) * p.Hq + kvh * p.g + (row - j * p.g)];
-        row_lse[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row that saw nothing weighs nothing
-        row_lim[r] = len - (p.qlen - 1 - j);
+        // a row that saw nothing weighs nothing, whatever it holds: no token is in its sight
+        const bool some = l != -INFINITY;
+        row_lse[r] = some ? -l * kLog2e : -INFINITY;
+        row_lim[r] = some ? len - (p.qlen - 1 - j) : INT_MIN;
+        if (!some && r < here) left_out = parts + 1;
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       bar_arrive(bar(BQF));
-      const int least = len - (p.qlen - 1 - r0 / p.g);  // every row of the part sees the tokens before it
+      int least = len - (p.qlen - 1 - r0 / p.g);  // every row of the part sees the tokens before it
       const int32_t* table = p.sh.table[shard] + (size_t)b * p.sh.max_blocks[shard];
       const size_t mrow = ((size_t)b * p.Hkv + kvh) * (size_t)p.cap;
       const unsigned long long scale2 = f2pack(p.sl2, p.sl2);
@@ -423,6 +428,7 @@ __global__ void __launch_bounds__(MassTc<KV, D>::kThreads, D == 576 ? 1 : 2)
       int phys = entry(t0);
       float w0 = mass(t0);
       if (!wait_warp(bar(BQF), parts & 1u, abort_flag, p.err)) return false;  // the other threads' row constants
+      if (left_out == parts + 1) least = INT_MIN;  // (here: as a part of the tiles' test it cost 4 % of a ragged window)
       for (int tile = t0; tile < t1; ++tile) {
         const int t = start + tile * kTcRows + tid;
         const bool there = phys >= 0 && phys < p.sh.nblk[shard];  // else its mass_out is left alone
