@@ -564,6 +564,8 @@ def dcp_kv_evict(desc: AttnDesc, shards, seq_lens: torch.Tensor, shard_starts: t
     if total_lens is not None:
         _check_shape(total_lens, i32, (B,), "total_lens", dev)
     _check(workspace, torch.uint8, "workspace")
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
     _check_err(err, dev)
     rc = load().dcp_kv_evict(ctypes.byref(desc._c), arr, N, seq_lens.data_ptr(), shard_starts.data_ptr(),
                              B, keep.data_ptr(), n_sink, n_recent, mass_in.data_ptr(), _ptr(pos_in),
