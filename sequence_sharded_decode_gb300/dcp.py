@@ -548,6 +548,9 @@ def dcp_kv_evict(desc: AttnDesc, shards, seq_lens: torch.Tensor, shard_starts: t
     B, N, dev = int(shard_starts.shape[0]), len(shards), shard_starts.device
     arr = _cache(desc, shards, dev, B)
     cap = int(mass_in.shape[-1]) if mass_in.dim() else 0
+    for name, count in (("n_sink", n_sink), ("n_recent", n_recent)):
+        if not -1 << 31 <= count < 1 << 31:
+            raise ValueError(f"{name} must fit 32 bits, got {count}")
     i32, rows = torch.int32, (B, desc.num_kv_heads, cap)
     _check_shape(shard_starts, i32, (B, N), "shard_starts", dev)
     _check_shape(seq_lens, i32, (B,), "seq_lens", dev)

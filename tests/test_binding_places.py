@@ -1,5 +1,5 @@
 """The eviction binding refuses what the library could not see: a workspace on
-another device (no GPU)."""
+another device, counts that do not fit its integers (no GPU)."""
 import types
 
 import pytest
@@ -34,9 +34,15 @@ def evict(monkeypatch):
 
 
 def test_a_good_call_reaches_the_library(evict):
-    assert len(evict()) == 1
+    assert len(evict()) == 1 and len(evict(n_sink=2 ** 31 - 1, n_recent=0)) == 2
 
 
 def test_a_workspace_on_another_device_is_refused(evict):
     with pytest.raises(ValueError, match="workspace"):
         evict(device=1)
+
+
+@pytest.mark.parametrize("kw", [dict(n_sink=2 ** 31), dict(n_recent=2 ** 32 + 3), dict(n_sink=-2 ** 32)])
+def test_counts_beyond_int32_are_refused(evict, kw):
+    with pytest.raises(ValueError, match="n_sink|n_recent"):
+        evict(**kw)
