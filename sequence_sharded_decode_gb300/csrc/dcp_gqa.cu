@@ -33,6 +33,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 11 bits down to 2^-29 of the maximum, 0 only below 2^-40 (with P at most 1,
 // tokens of 2^-25 of a heavy one counted as 0).
 constexpr float kF8Head = 15.f;
+constexpr float kF8Large = 4194304.f;  // log2 units
 constexpr float kLoFraction = 1.0f / 32.0f;  // F8: tile share of a row's weight above which P_lo . V is issued
 
 // F8: the cache holds FP8 E4M3 codes (1 byte per element) instead of bf16;
@@ -442,14 +443,14 @@ __global__ void __launch_bounds__(GqaCfg<D>::kThreads, (GqaCfg<D, F8, T>::kMinCt
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][e] *= p.sl2;
+          for (int e = 0; e < 4; ++e) s[h][e] = __fmul_rn(s[h][e], p.sl2);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = F8 ? 4 * t4 + 2 * h + (e & 1) : h * 8 + 2 * t4 + (e & 1);
-            s[h][e] = tok < ntok ? s[h][e] * p.sl2 : -INFINITY;
+            s[h][e] = tok < ntok ? (F8 ? __fmul_rn(s[h][e], p.sl2) : s[h][e] * p.sl2) : -INFINITY;
           }
         }
       }
@@ -464,7 +465,16 @@ __global__ void __launch_bounds__(GqaCfg<D>::kThreads, (GqaCfg<D, F8, T>::kMinCt
       const float c0 = n0 == -INFINITY ? 0.f : n0;
       const float c1 = n1 == -INFINITY ? 0.f : n1;
       const float a0 = exp2_k<F8>(m0 - c0), a1 = exp2_k<F8>(m1 - c1);
-      const float r0 = F8 ? c0 - kF8Head : c0, r1 = F8 ? c1 - kF8Head : c1;
+      float r0 = F8 ? c0 - kF8Head : c0, r1 = F8 ? c1 - kF8Head : c1;
+      // scores so large that rounding r0 moves them by half a binade (P must not
+      // leave fp16 by it): the maximum is subtracted exactly first
+      if (F8 && __any_sync(0xffffffffu, fmaxf(fabsf(c0), fabsf(c1)) > kF8Large)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[h][e] -= e < 2 ? c0 : c1;
+        r0 = r1 = -kF8Head;
+      }
       m0 = n0;
       m1 = n1;
       float p_[2][4];

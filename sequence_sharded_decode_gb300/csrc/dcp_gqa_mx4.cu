@@ -26,9 +26,10 @@
 // the round and leaves their P in shared memory as MMA operands; then every
 // warp multiplies all the round's P with the values of its own blocks. O is at
 // most 32 registers a thread that way instead of 64, and nothing is widened
-// twice. On 32 sequences x 32K tokens x 64/4 heads of 128: 193 us with
-// the merge; one warp doing all of a tile by itself 253, a warp per block,
-// four in a CTA, 202 (each P and each line of value codes is read four times).
+// twice. On 32 sequences x 32K tokens x 64/4 heads of 128: 197 us with the
+// merge (193 before P was held relative to each round, see below); one warp doing
+// all of a tile by itself 253, a warp per block, four in a CTA, 202 (each P and
+// each line of value codes is read four times).
 // The warps exchange the rows' maxima over the round's 64 tokens, and P is held
 // relative to them, so that fp16's range serves the round and not the row: a
 // row's light tokens (behind a sink, say, 2^-25 of it each) keep their bits. The
@@ -54,10 +55,10 @@
 // are 97 ns of an SM that way, where its share of HBM delivers the 2,176 bytes
 // in 49 ns. Lanes of at most eight rows (HALF: one query token of up to eight
 // heads per KV head, say) put P's low terms into the MMA's upper rows, which are
-// empty, and leave the upper rows' scores alone: 32 MMAs, 177 us where 16 rows
-// take 193 (32 x 32K tokens, 4 KV heads; D = 128 spills 22 bytes a thread).
-// More warps change nothing: 193 us at 12 an SM (168 registers), 203 at 16 (128
-// registers, two stages).
+// empty, and leave the upper rows' scores alone: 32 MMAs, 175 us where 16 rows
+// take 197 (32 x 32K tokens, 4 KV heads). More warps change nothing: 193 us at 12
+// an SM (168 registers), 203 at 16 (128 registers, two stages), both with P
+// relative to the row.
 #include <cmath>
 #include <mutex>
 
@@ -443,7 +444,9 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
 #pragma unroll
       for (int e = 0; e < kO; ++e) o[m][e] = 0.f;
     // the rows' references in log2 units and the sums of this lane's columns
-    float ref0 = kNone, ref1 = kNone, l[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    // (bar0: where ref0 rises, before the scale; 175 us instead of 177 for eight
+    // rows, but 202 instead of 197 for 16, whose registers are all taken)
+    float bar0 = kNone, ref0 = kNone, ref1 = kNone, l[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     // scale code of O's unit: of this warp's blocks, and of block gr % kBlk,
     // whose factors the lane makes; 15 or more, so that the codes within 14
     // below a unit are not negative
@@ -539,10 +542,8 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
                 else mx1 = fmaxf(mx1, s[j][h][e]);
               }
       }
-      // (a maximum of -inf is a row that sees none of the tokens; NaN, from a scale of 0, counts as that)
-      mx0 *= rsl2[0];
-      mx1 = HALF ? mx0 : mx1 * rsl2[1];
-      // (each lane's part of the maxima, for both warps: no shuffles before the barrier)
+      // each lane's part of the maxima, for both warps (no shuffles before the
+      // barrier); -inf: none of the tokens is in the row's sight
       red[(warp * 16 + gr) * 4 + t4] = mx0;
       if (!HALF) red[(warp * 16 + gr + 8) * 4 + t4] = mx1;
       // Value scales of block gr % kBlk, tokens 2 t4 and 2 t4 + 1 of either half:
@@ -571,24 +572,25 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
       }
       // every warp has left the round before (its P, factors and stage are free),
       // and knows whether a score is too high or a scale far from its unit
-      const bool high = __syncthreads_or(mx0 > ref0 + kRise || mx1 > ref1 + kRise || far != 0u);
+      const bool risen = HALF ? mx0 > bar0 : mx0 * rsl2[0] > ref0 + kRise || mx1 * rsl2[1] > ref1 + kRise;
+      const bool high = __syncthreads_or(risen || far != 0u);
       if (*abort_flag) {  // (raised before the barrier: the same for all)
         stopped = i;
         break;
       }
       if (i > 0 && i + C::kStages - 1 < n_rounds) issue(i + C::kStages - 1);
-      // the rows' maxima in this round
-      float x0 = kNone, x1 = kNone;
+      // the rows' maxima in this round, as they were summed and in log2 units
+      float s0 = kNone, s1 = kNone;
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
         const float4 a = *reinterpret_cast<const float4*>(red + (w * 16 + gr) * 4);
-        x0 = max3f(max3f(x0, a.x, a.y), a.z, a.w);
+        s0 = max3f(max3f(s0, a.x, a.y), a.z, a.w);
         if (!HALF) {
           const float4 c = *reinterpret_cast<const float4*>(red + (w * 16 + gr + 8) * 4);
-          x1 = max3f(max3f(x1, c.x, c.y), c.z, c.w);
+          s1 = max3f(max3f(s1, c.x, c.y), c.z, c.w);
         }
       }
-      if (HALF) x1 = x0;
+      const float x0 = s0 * rsl2[0], x1 = HALF ? x0 : s1 * rsl2[1];
       if (high) {
         int top = 0;
 #pragma unroll
@@ -615,6 +617,7 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
         const float a0 = ex2_ftz(ref0 - top0), a1 = ex2_ftz(ref1 - top1);
         ref0 = top0;
         ref1 = top1;
+        if (HALF) bar0 = (ref0 + kRise) / rsl2[0];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           l[0][e] *= a0;
@@ -653,19 +656,25 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
       }
       // P of this warp's tiles, 2^kHead at the round's maximum; in O's units that
       // is size0, size1 times as much
-      const float r0 = x0 - kHead, r1 = x1 - kHead;
-      const float size0 = ex2_ftz(r0 - ref0), size1 = ex2_ftz(r1 - ref1);
+      const float size0 = ex2_ftz((x0 - ref0) - kHead), size1 = ex2_ftz((x1 - ref1) - kHead);
       if (n0 + n1 > 0) {
         float sum0[2] = {0.f, 0.f}, sum1[2] = {0.f, 0.f};
         const unsigned long long f0 = f2pack(rsl2[0], rsl2[0]), f1 = f2pack(rsl2[1], rsl2[1]);
+        const float below[4] = {-s0, -s0, -s1, -s1}, head[2] = {kHead, kHead};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t pa[4], pl[4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float z[4] = {-r0, -r0, -r1, -r1};
+            // (the difference first, which is exact near the maximum: P does not
+            // leave fp16, however large the scores)
+            float z[4] = {head[0], head[1], head[0], head[1]};
+            add2(s[j][h], below);
             fma2(z, s[j][h], f0);
-            if (!HALF) fma2(z + 2, s[j][h] + 2, f1);
+            if (!HALF) {
+              add2(s[j][h] + 2, below + 2);
+              fma2(z + 2, s[j][h] + 2, f1);
+            }
 #pragma unroll
             for (int e = 0; e < (HALF ? 2 : 4); ++e) z[e] = ex2_ftz(z[e]);
             if (!whole) {

@@ -701,7 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t gt = 0;
     int n_q = 0, n_epi = 0;  // query loads, epilogues
     uint32_t n_pc = 0;       // pieces counted (one-call path)
-    float m_run = -INFINITY, l_half = 0.f;
+    float m_run = -INFINITY, l_half = 0.f, raw_ref = 0.f;  // raw_ref: m_run before the scale
     volatile int* merge_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 96);
     // F8: widen page G's codes (in the codes stage) to fp16, exactly (E4M3 is
     // a subset of fp16): part 0 the score-only boxes into the shared region,
@@ -868,23 +868,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool rescale = false;
         if (m_run == -INFINITY) {
           m_new = mx;
-        } else if (mx > m_run + (F8 ? kF8Threshold : kRescaleThreshold)) {
+          raw_ref = n_valid > 0 ? raw_ext : 0.f;
+        } else if (F8 ? (raw_ext - raw_ref) * p.sl2 > kF8Threshold : mx > m_run + kRescaleThreshold) {
           m_new = mx;
+          raw_ref = raw_ext;
           alpha = exp2f(m_run - m_new);
           rescale = true;
         }
-        const float ref = m_new == -INFINITY ? 0.f : F8 ? m_new - kF8Head : m_new;
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
         float sc[32];
         float lsum;
         {
-          // two scores scaled and shifted per instruction; the row sum in pairs
+          // two scores scaled and shifted per instruction; the row sum in pairs.
+          // F8: the difference to the reference before the scale, which is exact
+          // near it, so that P does not leave fp16 however large the scores
+          // (MLA long 771 -> 777 us; bf16's P has fp32's range).
           const int t0 = 32 * e;
-          const unsigned long long s2 = f2pack(p.sl2, p.sl2), r2 = f2pack(-ref, -ref);
+          const unsigned long long s2 = f2pack(p.sl2, p.sl2), r2 = F8 ? f2pack(kF8Head, kF8Head) : f2pack(-ref, -ref);
+          const unsigned long long below = f2pack(-raw_ref, -raw_ref);
           unsigned long long a0 = f2pack(0.f, 0.f), a1 = a0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            f2unpack(ffma2(f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), s2, r2), x0, x1);
+            unsigned long long y = f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+            if (F8) y = fadd2(y, below);
+            f2unpack(ffma2(y, s2, r2), x0, x1);
             sc[2 * i] = (t0 + 2 * i < n_valid) ? ex2_ftz(x0) : 0.f;
             sc[2 * i + 1] = (t0 + 2 * i + 1 < n_valid) ? ex2_ftz(x1) : 0.f;
             if (i & 1)

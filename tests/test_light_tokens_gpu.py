@@ -164,3 +164,56 @@ def test_uniform_queries_are_unchanged_by_a_common_offset():
         o, lse = c.attend(_query(1, hq, d, 16.0).cuda())
         assert np.abs(o[0].cpu().numpy() - values.mean(axis=0)).max() <= 3.0 * (2.0 ** -15 + (n + 8) * 2.0 ** -23)
         assert np.abs(lse[0].cpu().numpy() - (16.0 * size + math.log(n))).max() <= 1e-3 and c.flag() == 0
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("size", [1.1e3, 3.7e5, 1.3e7, 9.1e8])
+@pytest.mark.parametrize("kv,hq,hkv,d,bs,J", [("mxfp4", 8, 2, 64, 16, 1), ("mxfp4", 16, 1, 128, 16, 1), ("mxfp4", 4, 1, 128, 16, 5),
+                                              ("fp8", 8, 2, 64, 16, 1), ("fp8", 128, 1, 576, 64, 1), ("bf16", 16, 1, 128, 16, 1),
+                                              ("bf16", 128, 1, 576, 64, 1)])
+def test_scores_past_the_fractions_of_fp32(kv, hq, hkv, d, bs, J, size, sign):
+    """Scores whose spacing in fp32 is many binades: the largest ones share the weight, the others have none, and nothing
+    overflows on the way. The largest ones' tokens hold the same values: a sequence is cut into pieces whose weights
+    come from their fp32 LSEs, spaced 2^-5 (size 3.7e5) to 64 nats (9.1e8) here, so that the pieces' shares of the
+    weight are not determined, only their sum."""
+    n, dv = 500, 512 if d == 576 else d
+    g = np.random.default_rng(int(size))
+    key = sign * g.choice([0.5, 1.0, 1.5, 2.0, 3.0], (n, hkv))
+    top = [7, 300, 301, 470]                                     # in rounds, warps and shards of their own
+    key[top] = sign * 4.0
+    values = g.choice(GRID, (n, hkv, dv))
+    values[top] = values[7]
+    k, v = _rows(kv, n, hkv, d, key, values)
+    c = Cache(kv, [n], hq, hkv, d, bs, 2, [(k, v)], scale=sign * size / 3.0)
+    o, lse = c.attend(_query(J, hq, d, 0.75).cuda())
+    assert c.flag() == 0
+    want = np.repeat(values[7], hq // hkv, axis=0)
+    got = o[0].cpu().numpy()
+    assert np.abs(got - want).max() <= 3.0 * (REL[kv] + (n + 8) * 2.0 ** -23), np.abs(got - want).max()
+    assert np.abs(lse[0].cpu().numpy() - size).max() <= math.log(len(top)) + 2.0 ** -20 * size
+
+
+@pytest.mark.parametrize("kv,hq,hkv,d,bs", [("mxfp4", 8, 1, 64, 16), ("mxfp4", 16, 1, 128, 16), ("fp8", 8, 1, 64, 16),
+                                            ("fp8", 16, 1, 128, 16), ("fp8", 128, 1, 576, 64)])
+def test_large_scores_a_step_of_fp32_apart(kv, hq, hkv, d, bs):
+    """Scores near 2^30 that rise by single steps of fp32 (64 nats and more in all) from token to token, whose rounded
+    products with the scale may be equal: the outputs stay finite and within the values."""
+    n, dv = 400, 512 if d == 576 else d
+    g = np.random.default_rng(d)
+    at = 512 if d == 576 else 0
+    k = np.zeros((n, hkv, d))
+    k[..., at] = 4.0
+    k[..., at + 1] = np.linspace(-1, 1, n)[:, None]       # a few steps of fp32 beside the first product
+    values = g.choice(GRID, (n, hkv, dv))
+    if d == 576:
+        k[..., :512] = values
+    c = Cache(kv, [n], hq, hkv, d, bs, 1, [(_bf16(k), None if d == 576 else _bf16(values))], scale=1.43e9 / 4)
+    q = torch.zeros(1, 1, hq, d, dtype=torch.bfloat16)
+    q[..., at] = 1.0
+    q[..., at + 1] = torch.exp2(-torch.arange(hq) / 8 - 14).to(torch.bfloat16)
+    for sign in (1.0, -1.0):
+        o, lse = c.attend((q * sign).cuda())
+        got = o[0].cpu().numpy()
+        assert c.flag() == 0 and np.isfinite(got).all()
+        assert got.min() >= 1.0 - 2.0 ** -9 and got.max() <= 3.0 + 2.0 ** -7
+        assert np.abs(lse[0].cpu().numpy() - sign * 1.43e9).max() <= 2.0 ** 18
