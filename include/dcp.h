@@ -421,10 +421,10 @@ DCP_API size_t dcp_evict_workspace_size(const dcp_attn_desc* desc, int B, int N,
 
 /* Evict cached tokens, keeping the heaviest. Every (sequence b, shard i, KV
  * head h) holds n cached tokens and keeps k = min(max(keep[b,i], 0), n) of
- * them: first those among the first n_sink or the last n_recent positions,
- * then by mass, largest first; ties go to the lower cache index, a NaN mass
- * ranks as -inf. (Protected tokens rank as mass +inf, so if there are more
- * than k of them the lower cache indices stay.) Every shard evicts within its
+ * them by mass, largest first; the tokens among the first n_sink or the last
+ * n_recent positions rank as mass +inf, a NaN mass as -inf, and ties (among the
+ * protected tokens, and with a mass that is +inf) go to the lower cache index.
+ * Every shard evicts within its
  * own slice and every KV head chooses its own tokens; no row leaves its shard.
  *
  * The kept rows move, in place, to the shard's local indices [0, k): rows

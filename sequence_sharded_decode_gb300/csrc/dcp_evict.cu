@@ -1,10 +1,9 @@
 // Eviction from the cache by accumulated attention weight.
 //
 // Every lane -- (shard i, sequence b, KV head h), n cached tokens -- keeps
-// k = min(keep[b, i], n) tokens: the first n_sink and the last n_recent
-// positions before all others, then the largest mass; ties go to the lower
-// cache index, a NaN mass counts as -inf. The kept set is the same whatever
-// the order of the work.
+// k = min(keep[b, i], n) tokens of the largest mass; the first n_sink and the
+// last n_recent positions count as mass +inf, a NaN mass as -inf, and ties go to
+// the lower cache index. The kept set is the same whatever the order of the work.
 //
 // The kept rows end up at local indices [0, k) of their shard. Rows already
 // there stay; the kept rows behind (as many as there are holes before k) move
@@ -45,7 +44,10 @@
 namespace dcp {
 namespace {
 
-constexpr int kKeyCache = 25600;  // keys in shared memory: 100 KB, so that two CTAs fit an SM
+// Keys in shared memory: 100 KB, so that two CTAs of 512 threads fit an SM (the
+// form of 1024 threads, for fewer lanes than SMs, has the SM to itself and could
+// hold twice as many; not measured).
+constexpr int kKeyCache = 25600;
 constexpr int kMoveThreads = 256;
 
 struct EvictParams {

@@ -210,8 +210,8 @@ __device__ __forceinline__ float scale_value(uint32_t word, int b) {
 }
 
 // A lane's start (its queries, constants and first copies) takes a CTA about as
-// long as twelve tiles, which it counts for, before the lane's first (four
-// query tokens of 16 ragged sequences of up to 8K tokens in 4 shards: 53.6 us
+// long as twelve tiles, which it counts for, before the lane's first (measured on
+// one shape, for all of them: four query tokens of 16 ragged sequences of up to 8K tokens in 4 shards: 53.6 us
 // at 4, 44.7 at 8, 42.6 at 12, 42.9 at 16).
 constexpr int kLaneCost = 12;
 

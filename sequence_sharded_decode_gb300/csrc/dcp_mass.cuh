@@ -6,7 +6,7 @@
 // scan of the lengths (a few thousand integers from L2), so the lengths stay on
 // the device and the call is one launch. A lane counts kMassLaneCost tiles more
 // than it has, before its first: loading its query rows and constants takes a
-// CTA about as long as two tiles (16 ragged sequences of up to 8K tokens in 4
+// CTA about as long as two tiles (measured on one shape, for all of them: 16 ragged sequences of up to 8K tokens in 4
 // shards, 32 query tokens: 46 us at 1, 40 at 2 and 3, 43 at 5).
 #pragma once
 
