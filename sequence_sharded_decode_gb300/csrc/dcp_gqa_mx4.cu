@@ -77,8 +77,7 @@ constexpr float kHead = 14.f;
 // A row's reference, the unit of its O and sum, follows when a score is 2^kRise
 // above it. (fp32 has room for more; a rise costs a rescale of O.)
 constexpr float kRise = 40.f;
-// The reference of a row that has seen nothing: finite, so that differences of
-// two references are numbers or -inf, and 2^them 1 or 0.
+// A row that sees nothing: finite, so that differences are numbers or infinite.
 constexpr float kNone = -3e38f;
 
 template <int D>
@@ -655,8 +654,9 @@ __global__ void __launch_bounds__(Mx4Cfg<D>::kThreads, Mx4Cfg<D>::kMinCtas)
         if (lane == 0) tile_info[2 * warp + j] = (unsigned char)(n <= 0 ? 0 : n | (apart ? 128 : 0));
       }
       // P of this warp's tiles, 2^kHead at the round's maximum; in O's units that
-      // is size0, size1 times as much
-      const float size0 = ex2_ftz((x0 - ref0) - kHead), size1 = ex2_ftz((x1 - ref1) - kHead);
+      // is size0, size1 times as much (a row that sees nothing here has P 0, and x
+      // anywhere: the factor stays finite)
+      const float size0 = ex2_ftz(fminf(x0 - ref0, 100.f) - kHead), size1 = ex2_ftz(fminf(x1 - ref1, 100.f) - kHead);
       if (n0 + n1 > 0) {
         float sum0[2] = {0.f, 0.f}, sum1[2] = {0.f, 0.f};
         const unsigned long long f0 = f2pack(rsl2[0], rsl2[0]), f1 = f2pack(rsl2[1], rsl2[1]);

@@ -30,7 +30,8 @@
 //   1. S = Q . K^T (M=128 heads, N=64 tokens, K=576) into TMEM; query dims
 //      0-383 are the MMA's A operand in TMEM, dims 384-575 in shared memory
 //   2. online softmax per head row, in log2 units, lazy rescale of O (only
-//      when the running max grows by more than 2^8): eight warps, two per
+//      when the running max grows by more than 2^8, 2^4 over the 8-bit cache,
+//      whose P is fp16): eight warps, two per
 //      TMEM lane quadrant; both read all 64 scores of their rows and take the
 //      same maximum, each exponentiates its own 32 tokens and keeps their
 //      row sum; the two sums meet once per item, for the epilogue
@@ -868,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool rescale = false;
         if (m_run == -INFINITY) {
           m_new = mx;
-          raw_ref = n_valid > 0 ? raw_ext : 0.f;
+          raw_ref = mx == -INFINITY ? 0.f : raw_ext;
         } else if (F8 ? (raw_ext - raw_ref) * p.sl2 > kF8Threshold : mx > m_run + kRescaleThreshold) {
           m_new = mx;
           raw_ref = raw_ext;

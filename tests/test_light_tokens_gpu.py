@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle as O
-from compress_helpers import Cache, as_cached
+from compress_helpers import Cache, as_cached, queries
 from helpers import f64
 
 pytestmark = pytest.mark.gpu
@@ -217,3 +217,23 @@ def test_large_scores_a_step_of_fp32_apart(kv, hq, hkv, d, bs):
         assert c.flag() == 0 and np.isfinite(got).all()
         assert got.min() >= 1.0 - 2.0 ** -9 and got.max() <= 3.0 + 2.0 ** -7
         assert np.abs(lse[0].cpu().numpy() - sign * 1.43e9).max() <= 2.0 ** 18
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("hq,hkv,d,J", [(8, 2, 64, 1), (16, 1, 128, 1), (4, 1, 128, 4), (40, 1, 64, 2)])
+def test_a_bad_query_row_stays_by_itself(hq, hkv, d, J, bad):
+    """A row of NaN or infinities gives NaN, and the rows that share its lane what they give without it."""
+    lens = [300, 70]
+    g = torch.Generator().manual_seed(3)
+    rows = [tuple(torch.randn(n, hkv, d, generator=g).to(torch.bfloat16) for _ in range(2)) for n in lens]
+    c = Cache("mxfp4", lens, hq, hkv, d, 16, 2, rows)
+    q = queries(2, J, hq, d, 5)
+    o, lse = c.attend(q.cuda())
+    out = torch.zeros(2, J, hq, dtype=torch.bool)
+    out[0, 0, 1], out[1, J - 1, hq - 1] = True, True
+    q[out] = bad
+    o2, lse2 = c.attend(q.cuda())
+    out = out.cuda()
+    assert c.flag() == 0
+    assert torch.equal(o[~out], o2[~out]) and torch.equal(lse[~out], lse2[~out])
+    assert torch.isnan(o2[out]).all() and torch.isnan(lse2[out]).all()
