@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from dataclasses import dataclass
 
@@ -143,8 +144,12 @@ class Shard:
     def _form(self):
         """(library form, what it was made of, (device, pool type, table rows, elements of a key and a value block))"""
         made, k, v, t = self._made, self.k_pool, self.v_pool, self.block_table
-        now = (k.data_ptr(), None if v is None else v.data_ptr(), t.data_ptr(), k.shape, t.shape, k.dtype, t.dtype,
-               k.is_contiguous(), t.is_contiguous(), v is None or (v.shape, v.dtype, v.is_contiguous()))
+        # (strides and bytes stand for the shape, which takes longer to ask for)
+        if v is None:
+            now = (k.data_ptr(), t.data_ptr(), k.stride(), t.stride(), k.nbytes, t.nbytes, k.dtype, t.dtype)
+        else:
+            now = (k.data_ptr(), t.data_ptr(), k.stride(), t.stride(), k.nbytes, t.nbytes, k.dtype, t.dtype, v.data_ptr(),
+                   v.stride(), v.nbytes, v.dtype)
         if made is not None and made[1] == now:
             return made
         if k.dtype not in (torch.bfloat16, torch.uint8):
@@ -156,7 +161,7 @@ class Shard:
         devices = {x.device for x in (k, v, t) if x is not None}
         what = (devices.pop() if len(devices) == 1 else None, k.dtype, int(t.shape[0]) if t.dim() == 2 else -1,
                 tuple(k.shape[1:]), None if v is None else tuple(v.shape[1:]))
-        made = (_Shard(now[0], now[1], int(k.shape[0]), now[2], int(t.shape[1])), now, what)
+        made = (_Shard(now[0], None if v is None else now[8], int(k.shape[0]), now[1], int(t.shape[1])), now, what)
         self.__dict__["_made"] = made
         return made
 
@@ -230,12 +235,14 @@ def _ptr(t):
 
 # the current stream's handle without making a torch.cuda.Stream (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device without looking whether CUDA is up (the tensors are there)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -246,10 +253,22 @@ _SHARD_ARRAYS = [_Shard * n for n in range(DCP_MAX_SHARDS + 1)]
 
 
 def _shards(shards) -> ctypes.Array:
-    n = len(shards)
+    return _array(shards, [s._form() for s in shards])
+
+
+def _array(shards, forms) -> ctypes.Array:
+    """The library forms side by side: those of the last call, kept with the
+    first shard, if they are the same."""
+    n = len(forms)
+    if n == 0:
+        return _SHARD_ARRAYS[0]()
+    kept = shards[0].__dict__.get("_array")
+    if kept is not None and len(kept[0]) == n and all(map(operator.is_, kept[0], forms)):
+        return kept[1]
     arr = (_SHARD_ARRAYS[n] if n <= DCP_MAX_SHARDS else _Shard * n)()
-    for i, s in enumerate(shards):
-        arr[i] = s._form()[0]
+    for i, form in enumerate(forms):
+        arr[i] = form[0]
+    shards[0].__dict__["_array"] = (forms, arr)
     return arr
 
 
@@ -454,19 +473,16 @@ def _cache(desc: AttnDesc, shards, device, batch: int) -> ctypes.Array:
     types and shapes and one device, the current one."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    n = len(shards)
-    arr = (_SHARD_ARRAYS[n] if n <= DCP_MAX_SHARDS else _Shard * n)()
+    if device.index != _current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
     want = (device, desc.kv_torch_dtype, batch, *desc.block_shapes)
-    for i, s in enumerate(shards):
-        form = s._form()
-        arr[i] = form[0]
+    forms = [s._form() for s in shards]
+    for i, form in enumerate(forms):
         if form[2] != want:
             for name, got, need in zip(("device", "pool type", "block_table rows", "k_pool block", "v_pool block"), form[2], want):
                 if got != need:
                     raise ValueError(f"shards[{i}]: {name} must be {need}, got {got}")
-    return arr
+    return _array(shards, forms)
 
 
 def _check_err(err, device):
